@@ -603,7 +603,10 @@ dspark_status_t dspark_backbone_block(const int32_t *tokens, int B, int nr, cons
  * Query rows q, out [B, nr, nq, 128] bf16: row i of request b stands at position
  * p = lens[b] - nr + i (its own key is the cache's last nr keys' i-th).  A row that
  * sees no key gives zeros.  Scores are fp32 (scaled by 1/sqrt(128)), softmax statistics
- * and sums fp32, outputs rounded once to bf16.  Results do not depend on timing.
+ * and sums fp32, outputs rounded once to bf16.  The softmax weights enter the sum over the
+ * values as two bf16 parts (2^-16 relative) where at most 64 query rows share a kv head's
+ * keys (nr * nq / nkv; for the keys of a shared prefix B * nr * nq / nkv), else rounded to
+ * bf16 once (each off by up to 2^-8 relative).  Results do not depend on timing.
  * Outputs must not overlap inputs except where a call says so.
  * Limits: nq % nkv == 0, nq <= 4096, nkv <= 1024, B <= 2^16, B * nr <= 2^20,
  * cache_len <= 2^30.

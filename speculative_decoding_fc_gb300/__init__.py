@@ -935,7 +935,9 @@ def window_attention(q, k_cache, v_cache, lens, window, sinks=0, causal=False, o
     """Attention of q [B, nr, nq, 128] over the first lens[b] keys of each request's cache:
     row i, at position p = lens[b] - nr + i, sees key t iff t < sinks or t > p - window
     (window None or 0: every key) and, when causal, t <= p.  lens: int32 [B] on the device.
-    Any nr; rows that see no key give zeros.  Returns out [B, nr, nq, 128] bf16."""
+    Any nr; rows that see no key give zeros.  Weights enter P V as two bf16 parts up to 64
+    rows per kv head (nr * nq / nkv), rounded to bf16 once above.  Returns out [B, nr, nq,
+    128] bf16."""
     di = _index(q, "q")
     B, nr, nq, nkv, cache_len, (qp, kp, vp, lp) = _ragged_args(q, k_cache, v_cache, lens, out, di)
     with _on(di, stream):
@@ -953,7 +955,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, lens, causa
     """Attention of q [B, nr, nq, 128] over a prefix all requests share (k_prefix, v_prefix
     [P, nkv, 128], read once for the whole batch) and each request's own first lens[b] keys
     (k_cache, v_cache [B, cache_len, nkv, 128]; causal: row i sees own keys up to
-    lens[b] - nr + i).  Returns out [B, nr, nq, 128] bf16."""
+    lens[b] - nr + i).  The prefix's weights are rounded as window_attention's with
+    B * nr * nq / nkv rows.  Returns out [B, nr, nq, 128] bf16."""
     di = _index(q, "q")
     B, nr, nq, nkv, cache_len, (qp, kp, vp, lp) = _ragged_args(q, k_cache, v_cache, lens, out, di)
     P = k_prefix.shape[0]

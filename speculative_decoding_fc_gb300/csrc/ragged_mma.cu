@@ -59,7 +59,7 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
 // end.  16 rows are one warp-level MMA's height; the tcgen05 MMA's is 128, and with 5 rows
 // of a group there would be nothing but padding in it, which costs its softmax's registers
 // and latency.  Scores: bf16 q and k, fp32 sums, log2 units (scaled by log2(e) / sqrt(128)
-// after the sum).  The weights enter P.V as bf16 parts hi + lo (2^-17 relative; the kernel
+// after the sum).  The weights enter P.V as bf16 parts hi + lo (2^-16 relative; the kernel
 // waits for memory, the second product costs nothing), the value rows exact.
 // One thread issues a tile's loads (TMA, four boxes of 64 keys x 64 dims in 128-byte
 // swizzle, which ldmatrix reads without conflicts): copies issued by every thread

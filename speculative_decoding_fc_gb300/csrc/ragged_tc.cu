@@ -18,11 +18,11 @@
 //                   swizzle), O += P V (P from tensor memory, V as its N-major operand: the
 //                   tile is used as it was loaded, nothing is transposed).
 // Tensor memory (512 columns): per half S (64 fp32 columns), two buffers of P (64 bf16, 32
-// columns each) and O (128).  Q K^T of tile t + 1 runs as soon as the softmax has read S of
-// tile t, P V of tile t when its weights are there, so the tensor pipe has work while the
-// softmax computes.  (With tiles of 128 keys S filled its half's columns, P had to take its
-// place, and products and softmax of a half took turns: 3500 cycles per 128 keys of both
-// halves, of which the pipe worked 2050.)
+// columns each; streams: P's two parts) and O (128).  Q K^T of tile t + 1 runs as soon as the
+// softmax has read S of tile t, P V of tile t when its weights are there, so the tensor pipe has
+// work while the softmax computes.  (With tiles of 128 keys S filled its half's columns, P had
+// to take its place, and products and softmax of a half took turns: 3500 cycles per 128 keys
+// of both halves, of which the pipe worked 2050.)
 // Measured: 1536 rows of 40 heads over a prefix of 32749 keys, 1.03 TFLOP in 733 us: 1.40
 // PFLOP/s, 72% of the bf16 peak measured with a large library product; 1710 cycles per 64
 // keys of both halves, in which the pipe has 1024 of work and a softmax about 1100.  What
@@ -32,8 +32,17 @@
 // the ring's stages given back by the softmax warps instead of a commit each.
 // The output is rescaled only when a row's maximum has grown by more than 2^8 since the
 // last time (weights up to 2^8 lose nothing in fp32 sums or bf16 weights), which after the
-// first tiles is rare.  Weights are rounded to bf16 once (half a step, 2^-8 relative, each
-// rounding its own way); their sum is taken in fp32 before the rounding.
+// first tiles is rare.  The weights' sum is taken in fp32, before they are rounded.
+// Streams form: the weights enter P V as bf16 parts hi + lo (2^-16 relative), as in the decode
+// kernel and the backbone's attention, so that the same block gets the same bits of accuracy
+// through any of them.  The second product's 256 cycles a tile are free where the keys'
+// reading is the bound; the parts take both of P's buffers, so a tile's weights wait for the
+// product before (draft block over 1032 keys 11.6 -> 12.0 us, 4 tokens over a prefix of
+// 4096 15.7 -> 16.5).
+// Shared form: rounded to bf16 once (half a step, 2^-8 relative, each rounding its own way: an
+// output's error grows from 0.0017 to 0.0018 relative, most of it the output's own rounding).
+// With two parts a prompt of 2 x 4099 tokens took 394 us for 334, 32 x 8 queries over a
+// prefix of 16384 115 for 99, and 192 x 8 over 32749 1140 for 900.
 // Value rows of keys that no row of the item sees are left out of P V in steps of 16 keys;
 // those in a step with seen keys are zeroed in shared memory first (their weights are
 // zero, but they may hold NaN or infinities).
@@ -426,11 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_tc_kernel(const __grid_con
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t v_lo = desc_lo(ring + vs * kTileBytes, kDescV), pt = tp + b * 32;
+            const uint32_t v_lo = desc_lo(ring + vs * kTileBytes, kDescV), pt = kTwo ? tp : tp + b * 32;
             if (steps == 0xfu) {
 #pragma unroll
-              for (int kk = 0; kk < kKT / 16; ++kk)
-                mma_ts(to, pt + kk * 8, v_lo + kk * (2048 >> 4), kIdescPV, t > 0 || kk > 0);
+              for (int part = 0; part < (kTwo ? 2 : 1); ++part)
+#pragma unroll
+                for (int kk = 0; kk < kKT / 16; ++kk)
+                  mma_ts(to, pt + part * 32 + kk * 8, v_lo + kk * (2048 >> 4), kIdescPV, t > 0 || part > 0 || kk > 0);
             } else {
               bool acc = t > 0;
 #pragma unroll 1
@@ -438,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_tc_kernel(const __grid_con
                 if ((steps >> kk) & 1u) {
                   mma_ts(to, pt + kk * 8, v_lo + kk * (2048 >> 4), kIdescPV, acc);
                   acc = true;
+                  if (kTwo) mma_ts(to, pt + 32 + kk * 8, v_lo + kk * (2048 >> 4), kIdescPV, true);
                 }
             }
             tc_commit(pdone0 + 16 * h + 8 * b);
@@ -634,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_tc_kernel(const __grid_con
             }
             const float nm = m == -INFINITY ? 0.0f : -m;
             float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+            uint32_t low[kTwo ? kKT / 2 : 1];
 #pragma unroll
             for (int c = 0; c < kKT; c += 4) {
               float e[4];
@@ -647,12 +660,28 @@ __global__ void __launch_bounds__(kThreads, 1) ragged_tc_kernel(const __grid_con
               add2(s2, s3, e[2], e[3]);
               sr[c / 2] = pack_bf16(e[0], e[1]);
               sr[c / 2 + 1] = pack_bf16(e[2], e[3]);
+              if (kTwo) {
+                low[c / 2] = pack_bf16(e[0] - bf16_lo(sr[c / 2]), e[1] - bf16_hi(sr[c / 2]));
+                low[c / 2 + 1] = pack_bf16(e[2] - bf16_lo(sr[c / 2 + 1]), e[3] - bf16_hi(sr[c / 2 + 1]));
+              }
             }
             l += (s0 + s1) + (s2 + s3);
-            // (this buffer's last tile, the one before last, has been added to O: its P V was
-            // issued before this tile's Q K^T, whose commit covers it)
-            tmem_st16(tp + (count & 1) * 32, sr);
-            tmem_st16(tp + (count & 1) * 32 + 16, sr + 16);
+            if (kTwo) {
+              // hi and lo fill both buffers: the tile before has to be added to O first (an
+              // item's first tile: the item before was finished)
+              if (t > 0) ok = added(count - 1);
+              if (!ok) break;
+              tc_fence_after();
+              tmem_st16(tp, sr);
+              tmem_st16(tp + 16, sr + 16);
+              tmem_st16(tp + 32, low);
+              tmem_st16(tp + 48, low + 16);
+            } else {
+              // (this buffer's last tile, the one before last, has been added to O: its P V was
+              // issued before this tile's Q K^T, whose commit covers it)
+              tmem_st16(tp + (count & 1) * 32, sr);
+              tmem_st16(tp + (count & 1) * 32 + 16, sr + 16);
+            }
             tmem_wait_st();
           }
           tc_fence_before();

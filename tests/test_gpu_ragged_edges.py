@@ -1,0 +1,47 @@
+"""Ragged-batch operators where their kernels and schedules change: weights in two parts.
+
+Tolerances as derived in test_gpu_ragged.py, for weights of two bf16 parts: the low part
+is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together.  Both
+parts' products are added in fp32, 2 n additions over n keys:
+  |err| <= 2^-8 |out| (1 + w) + w sum p|v|,  w = 260 u A + 2^-16 + 2^-19 + 2 n u.
+"""
+import pytest
+import torch
+
+import ragged_ref as ref
+import speculative_decoding_fc_gb300 as ds
+from test_gpu_ragged import HD, U, _gen, _hide, _lens, _normal
+
+pytestmark = pytest.mark.gpu
+
+
+def _close2(out, want, av, a, n):
+    w = 260 * U * a + 2.0 ** -16 + 2.0 ** -19 + 2 * n * U
+    bound = 2.0 ** -8 * want.abs() * (1 + w) + w * av + 1e-30
+    assert torch.isfinite(out).all()
+    worst = ((out.double() - want).abs() / bound).max().item()
+    assert worst <= 1.0, "error %.3g of the bound" % worst
+
+
+PARTS_CASES = [
+    # nr, nq, nkv, cache, lens, window, sinks, causal: 17 to 64 rows per kv head
+    (8, 40, 8, 1100, [1032, 8, 5, 0], 512, 4, False),
+    (8, 40, 8, 5000, [4999, 2500, 129, 8], 0, 0, True),
+    (17, 4, 4, 300, [300, 64, 63, 65, 1], 0, 0, True),
+    (64, 2, 2, 700, [699, 64, 128], 33, 70, True),
+    (1, 40, 1, 2000, [2000, 1], 0, 0, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PARTS_CASES)))
+def test_weights_of_blocks_have_two_parts(case):
+    nr, nq, nkv, cache, lens, window, sinks, causal = PARTS_CASES[case]
+    g = _gen(1000 + case)
+    B = len(lens)
+    q = _normal((B, nr, nq, HD), g, 1.5)
+    kc, vc = _normal((B, cache, nkv, HD), g), _normal((B, cache, nkv, HD), g)
+    _hide(kc, vc, nr, lens, window, sinks, causal)
+    want, av, a = ref.window(q, kc, vc, lens, window, sinks, causal)
+    _close2(ds.window_attention(q, kc, vc, _lens(lens), window, sinks=sinks, causal=causal), want, av, a, cache)
+    if not window:
+        _close2(ds.attention_scored(q, kc, vc, _lens(lens), causal=causal)[0], want, av, a, cache)
