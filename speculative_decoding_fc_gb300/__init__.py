@@ -222,7 +222,9 @@ class Workspaces:
     """Zero-initialised device workspaces, one per (call kind, device), grown on
     demand.  Calls that share a workspace must be ordered on the GPU (one stream,
     or events); pass a separate Workspaces object to run calls concurrently.  A buffer
-    that was outgrown stays allocated: a captured graph may still write to it."""
+    that was outgrown stays allocated until release(): a captured graph, or work on
+    another stream, may still write to it.  Buffers at least double when they grow, so
+    that all outgrown ones together are smaller than the one in use."""
 
     def __init__(self):
         self._bufs = {}
@@ -240,11 +242,24 @@ class Workspaces:
         key = (kind, torch.device(device).index)
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
+            nbytes = max(int(nbytes), 256)
+            new = None
+            if buf is not None and 2 * buf.numel() > nbytes:
+                try:
+                    new = torch.zeros(2 * buf.numel(), dtype=torch.uint8, device=device)
+                except torch.cuda.OutOfMemoryError:
+                    pass   # what the call needs may still fit
+            if new is None:
+                new = torch.zeros(nbytes, dtype=torch.uint8, device=device)
             if buf is not None:
                 self._outgrown.append(buf)
-            buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-            self._bufs[key] = buf
+            buf = self._bufs[key] = new
         return buf
+
+    def release(self):
+        """Frees the outgrown buffers.  The caller sees to it that the calls which used them
+        have ended and that no graph captured with them is replayed again."""
+        self._outgrown.clear()
 
 
 _default_ws = Workspaces()
