@@ -619,8 +619,8 @@ dspark_status_t dspark_backbone_block(const int32_t *tokens, int B, int nr, cons
  * shared prefix).  pos, slot, nrows [B] int32 on the device; slot == NULL: pos; nrows ==
  * NULL: rows_per_req.  Rows past nrows[b] are left alone (q_out and caches).  Recorded in
  * *status (device int32 or NULL) as DSPARK_ERR_INVALID_ARG: a slot outside [0, cache_len)
- * (the row's k and v are not stored), a negative pos (taken as 0), an nrows outside
- * [0, rows_per_req].  nq == 0: keys and values only.  One kernel, no workspace. */
+ * (the row's k and v are not stored), a negative pos (taken as 0 for the rotation; with slot
+ * == NULL none of the request's k and v are stored), an nrows outside [0, rows_per_req].  nq == 0: keys and values only.  One kernel, no workspace. */
 dspark_status_t dspark_qk_norm_rope_ragged(const dspark_bf16_t *qkv, int64_t ld, int nq, int nkv,
                                            const dspark_bf16_t *q_norm_w, const dspark_bf16_t *k_norm_w, float theta,
                                            const int32_t *pos, const int32_t *slot, const int32_t *nrows,

@@ -897,8 +897,8 @@ def _ws(workspaces, kind, index, call, *sizes):
 def qk_norm_rope_ragged(qkv, nq, nkv, q_norm_w, k_norm_w, theta, k_cache, v_cache, rows_per_req, pos, slot=None,
                         nrows=None, q_out=None, status=None, stream=None):
     """qk_norm_rope with each request at its own place: row j < nrows[b] of request b is at
-    position pos[b] + j and its key and value go to cache slot slot[b] + j (slot None: pos;
-    nrows None: rows_per_req).  pos, slot, nrows: int32 [B] on the device.  Returns q
+    position pos[b] + j and its key and value go to cache slot slot[b] + j (slot None: pos,
+    nothing of a request at a negative one; nrows None: rows_per_req).  pos, slot, nrows: int32 [B] on the device.  Returns q
     [rows, nq, 128] (None when nq == 0); rows past nrows[b] are left alone (a fresh q_out
     holds zeros there).  status: optional int32 [1] that records bad places."""
     if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype is not _BF16 or qkv.dim() != 2 \

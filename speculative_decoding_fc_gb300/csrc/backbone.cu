@@ -367,7 +367,9 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_ragged_kernel(co
   if (j >= n) return;
   int p0 = __ldcg(a.pos + b);
   const long long slot = static_cast<long long>(a.slot ? __ldcg(a.slot + b) : p0) + j;
-  const bool store = slot >= 0 && slot < a.cache_len;   // a row without a slot is not stored
+  // a row without a slot is not stored; no slots given, a request at a negative position has none
+  // (its rows from -p0 on would land on live keys)
+  const bool store = slot >= 0 && slot < a.cache_len && (a.slot || p0 >= 0);
   if (tid == 0 && blockIdx.y == 0 && (!store || p0 < 0)) record_error(a.status, DSPARK_ERR_INVALID_ARG);
   if (p0 < 0) p0 = 0;
   if (tid < kHeadDim / 2) {

@@ -1,4 +1,5 @@
-"""Ragged-batch operators where their kernels and schedules change: weights in two parts.
+"""Ragged-batch operators where their kernels and schedules change: weights in two parts,
+places without a slot.
 
 Tolerances as derived in test_gpu_ragged.py, for weights of two bf16 parts: the low part
 is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together.  Both
@@ -45,3 +46,27 @@ def test_weights_of_blocks_have_two_parts(case):
     _close2(ds.window_attention(q, kc, vc, _lens(lens), window, sinks=sinks, causal=causal), want, av, a, cache)
     if not window:
         _close2(ds.attention_scored(q, kc, vc, _lens(lens), causal=causal)[0], want, av, a, cache)
+
+
+def test_negative_position_without_slots():
+    """No slot given: a request at a negative position has none, and nothing of it is stored."""
+    g = _gen(1500)
+    B, rows, nq, nkv, cache = 3, 8, 4, 2, 32
+    kc, vc = _normal((B, cache, nkv, HD), g), _normal((B, cache, nkv, HD), g)
+    k0, v0 = kc.clone(), vc.clone()
+    qkv = _normal((B * rows, (nq + 2 * nkv) * HD), g)
+    w = torch.ones(HD, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pos = [5, -3, 2]
+    q = ds.qk_norm_rope_ragged(qkv, nq, nkv, w, w, 1e6, kc, vc, rows, _lens(pos), status=st)
+    assert int(st.item()) == -1
+    assert torch.equal(kc[1], k0[1]) and torch.equal(vc[1], v0[1])
+    x = qkv.view(B, rows, nq + 2 * nkv, HD)
+    for b, p in enumerate([5, 0, 2]):   # queries: a negative position counts as 0
+        at = torch.arange(rows, device="cuda") + p
+        want, mag = ref.rope(x[b, :, :nq], w, at, 1e6)
+        assert ((q.view(B, rows, nq, HD)[b].double() - want).abs() <= 2.0 ** -8 * want.abs() + 64 * U * mag).all()
+        if b != 1:
+            want, mag = ref.rope(x[b, :, nq:nq + nkv], w, at, 1e6)
+            assert ((kc[b, p:p + rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + 64 * U * mag).all()
+            assert torch.equal(vc[b, p:p + rows], x[b, :, nq + nkv:])
