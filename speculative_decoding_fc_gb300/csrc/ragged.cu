@@ -169,9 +169,10 @@ dspark_status_t launch(Kind kind, const Call &c, void *ws, cudaStream_t stream) 
   part.fill(a, p);
   p += part.total;
   Args pre = a;   // the prefix's own launch
-  a.late_wait = apart;
+  a.late_wait = apart ? 1 : 0;
   if (apart) {
     pre.sB = 0;
+    pre.ordinary = 1;   // (the launch behind it does not wait: ragged.cuh, wait_first)
     pre.PRT = static_cast<int>(row_tiles(kShared, a.prows));
     const Part pp(kShared, c.nkv, 0, pre.PRT);
     pre.groups = range_count(kShared, sms, c.nkv);

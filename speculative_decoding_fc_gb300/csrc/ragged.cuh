@@ -112,16 +112,21 @@ struct Args {
   int sB;                               // requests in the launch's schedule (B, or 0: the prefix alone)
   int groups;                           // ranges the launch has CTAs for
   int direct;                           // no plan: every warp works its range out itself (WarpPlan)
-  int late_wait;                        // the kernel before is the prefix's own launch (wait_first, wait_last)
+  int late_wait;                        // the launch before is the prefix's own (wait_first, wait_last)
+  int ordinary;                         // this launch starts when everything before it has ended
   float scale_log2;                     // log2(e) / sqrt(128)
   int *status;
 };
 
-// The launch over the own keys after one over the prefix reads nothing of that one's, and it
-// starts only when all of that one's CTAs have waited for everything earlier (the plan): it
-// fills the SMs that the prefix's last CTAs leave.  It ends behind it, so that the join, which
-// waits for this launch alone, finds both complete.  32 x 8 queries over a prefix of
-// 16384: 108 us -> 98.
+// The launch over the own keys after one over the prefix reads nothing of that one's and does
+// not wait for it: it fills the SMs that the prefix's last CTAs leave.  What it does read (the
+// plan, q, the lengths, the caches) it may read without a wait of its own because the prefix's
+// launch is an ordinary one: that grid starts when everything before it in the stream has ended,
+// with its writes visible to whatever starts later, and a programmatic launch overlaps with the
+// one launch before it only.  (Behind a programmatic launch of the prefix it would rest on that
+// grid's waits, which promise visibility to that grid alone.)  It ends behind the prefix's
+// launch, so that the join, which waits for this launch, finds both complete.  32 x 8
+// queries over a prefix of 16384: 108 us -> 101 (the ordinary launch costs 1 of them).
 __device__ __forceinline__ void wait_first(const Args &a) {
   if (!a.late_wait) pdl_wait();
 }

@@ -763,7 +763,8 @@ dspark_status_t tc_launch(const Args &a, Form form, cudaStream_t stream) {
     done[streams][dev] = true;
   }
   const int ctas = (streams ? (a.groups + 1) / 2 : a.groups) * a.nkv;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, stream, prm) != cudaSuccess)
+  if (launch_kernel(!a.ordinary, kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, stream, prm) !=
+      cudaSuccess)
     return DSPARK_ERR_CUDA;
   count_launches(1);
   return DSPARK_OK;

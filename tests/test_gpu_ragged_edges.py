@@ -1,5 +1,5 @@
 """Ragged-batch operators where their kernels and schedules change: weights in two parts,
-places without a slot.
+places without a slot, data written right before a call.
 
 Tolerances as derived in test_gpu_ragged.py, for weights of two bf16 parts: the low part
 is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together.  Both
@@ -46,6 +46,46 @@ def test_weights_of_blocks_have_two_parts(case):
     _close2(ds.window_attention(q, kc, vc, _lens(lens), window, sinks=sinks, causal=causal), want, av, a, cache)
     if not window:
         _close2(ds.attention_scored(q, kc, vc, _lens(lens), causal=causal)[0], want, av, a, cache)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("B,nr,nq,nkv,P,cache", [(16, 8, 40, 8, 1500, 600), (80, 1, 20, 4, 3000, 300)])
+def test_shared_prefix_of_data_written_right_before(B, nr, nq, nkv, P, cache, graph):
+    """The launch over the own keys starts beside the prefix's: q, the lengths, the prefix and
+    the caches, written on the device directly before each call, are the call's."""
+    g = _gen(1400 + B)
+    bufs = [torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in
+            ((B, nr, nq, HD), (P, nkv, HD), (P, nkv, HD), (B, cache, nkv, HD), (B, cache, nkv, HD))]
+    lens = torch.empty(B, dtype=torch.int32, device="cuda")
+    sets, want = [], []
+    for i in range(4):
+        new = [_normal(b.shape, g, 1.5) for b in bufs]
+        n = _lens([(31 * b + 17 * i * i) % (cache + 1) for b in range(B)])
+        sets.append((new, n))
+        torch.cuda.synchronize()
+        want.append(ds.shared_prefix_attention(new[0], *new[1:], n, causal=True))
+        torch.cuda.synchronize()
+
+    def step(new, n):
+        for b, x in zip(reversed(bufs), reversed(new)):   # q last
+            torch.mul(x, 1.0, out=b)
+        torch.mul(n, 1, out=lens)
+        return ds.shared_prefix_attention(bufs[0], *bufs[1:], lens, causal=True)
+
+    def rounds():
+        return [step(*sets[i % 4]) for i in range(8)]
+
+    got = rounds()
+    if graph:
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            got = rounds()
+        captured.replay()
+        captured.replay()
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 4])
 
 
 def test_negative_position_without_slots():
