@@ -23,6 +23,7 @@ Ragged batches (requests of different lengths) of the drafter backbone:
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -870,6 +871,14 @@ def _dense(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _int(x, name):
+    """An int that the library takes in 32 bits (ctypes would cut larger ones off)."""
+    x = operator.index(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError("%s is %d: it must fit 32 bits" % (name, x))
+    return x
+
+
 def _index(t, name):
     """The device of a call: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
@@ -950,9 +959,10 @@ def window_attention(q, k_cache, v_cache, lens, window, sinks=0, causal=False, o
     """Attention of q [B, nr, nq, 128] over the first lens[b] keys of each request's cache:
     row i, at position p = lens[b] - nr + i, sees key t iff t < sinks or t > p - window
     (window None or 0: every key) and, when causal, t <= p.  lens: int32 [B] on the device.
-    Any nr; rows that see no key give zeros.  Weights enter P V as two bf16 parts up to 64
-    rows per kv head (nr * nq / nkv), rounded to bf16 once above.  Returns out [B, nr, nq,
-    128] bf16."""
+    window and sinks up to 2^30.  Any nr; rows that see no key give zeros.  Weights enter
+    P V as two bf16 parts up to 64 rows per kv head (nr * nq / nkv), rounded to bf16 once
+    above.  Returns out [B, nr, nq, 128] bf16."""
+    window, sinks = _int(int(window or 0), "window"), _int(sinks, "sinks")
     di = _index(q, "q")
     B, nr, nq, nkv, cache_len, (qp, kp, vp, lp) = _ragged_args(q, k_cache, v_cache, lens, out, di)
     with _on(di, stream):
@@ -960,7 +970,7 @@ def window_attention(q, k_cache, v_cache, lens, window, sinks=0, causal=False, o
             out = torch.empty_like(q)
         ws, nbytes = _ws(workspaces, "ragged_window", di, "dspark_window_attention", B, nr, nq, nkv)
         _check(lib().dspark_window_attention(qp, kp, vp, lp, out.data_ptr(), B, nr, nq, nkv, cache_len,
-                                             int(window or 0), sinks, 1 if causal else 0, ws, nbytes,
+                                             window, sinks, 1 if causal else 0, ws, nbytes,
                                              _raw_stream(di)), "dspark_window_attention")
     return out
 
@@ -1019,6 +1029,7 @@ def cache_evict(k_cache, v_cache, scores, lens, budget, sinks=0, recent=0, k_out
     and scores.  Into k_out, v_out [B, out_len, nkv, 128] and scores_out [B, nkv, out_len] (all
     three given), else in place; slots from m on are left alone.  Returns (new_lens [B] int32,
     kept [B, nkv, budget] int32: the old slots, then -1)."""
+    budget, sinks, recent = _int(budget, "budget"), _int(sinks, "sinks"), _int(recent, "recent")
     di = _index(k_cache, "k_cache")
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [B, cache_len, nkv, 128]")
