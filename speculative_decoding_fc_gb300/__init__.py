@@ -858,6 +858,8 @@ def _on(index, stream):
     """The calls below allocate (outputs, workspaces) and launch inside this context: on the
     tensors' device and on the stream the kernels run on."""
     if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, index))
         return torch.cuda.stream(stream)
     return _here if index == torch.cuda.current_device() else torch.cuda.device(index)
 

@@ -21,3 +21,11 @@ def test_sizes_past_32_bits_are_refused_not_cut_off(x):
                  lambda: ds.cache_evict(kc, kc, sc, lens, 8, recent=x)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        ds._on(0, Stream())
