@@ -831,7 +831,8 @@ dspark_status_t dspark_qk_norm_rope_ragged(const dspark_bf16_t *qkv, int64_t ld,
                                            int cache_len, int rows_per_req, int32_t *status, void *stream) {
   if (!qkv || !k_norm_w || !pos || !k_cache || !v_cache || (nq > 0 && (!q_out || !q_norm_w)))
     return DSPARK_ERR_INVALID_ARG;
-  if (nq < 0 || nkv < 1 || B < 1 || rows_per_req < 1 || cache_len < 1 || !(theta > 1.0f)) return DSPARK_ERR_INVALID_ARG;
+  if (nq < 0 || nkv < 1 || B < 1 || rows_per_req < 1 || cache_len < 1 || !(theta > 1.0f) || !std::isfinite(theta))
+    return DSPARK_ERR_INVALID_ARG;
   if (nq > 4096 || nkv > 1024 || cache_len > kMaxCacheLen || static_cast<long long>(B) * rows_per_req > kMaxM)
     return DSPARK_ERR_UNSUPPORTED_SHAPE;
   if (!ld_ok(ld, (nq + 2 * nkv) * 128)) return DSPARK_ERR_INVALID_ARG;
