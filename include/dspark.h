@@ -669,7 +669,8 @@ dspark_status_t dspark_attention_scored(const dspark_bf16_t *q, const dspark_bf1
  * with, and new keys go on at slot m (dspark_qk_norm_rope_ragged with slot != pos).
  *   k_out, v_out [B, out_len, nkv, 128], scores_out [B, nkv, out_len], out_len >=
  *     min(budget, cache_len): separate memory, or all three the inputs themselves (in
- *     place, out_len == cache_len); slots from m on are left alone;
+ *     place, out_len == cache_len); slots from m on are left alone.  No output overlaps an
+ *     input otherwise, or another output;
  *   new_lens [B] int32 (not lens itself); kept [B, nkv, budget] int32: the old slots, then
  *     -1.  sinks + recent <= budget, cache_len <= 2^22.  status: a device int32 or NULL.
  * Two kernels, no workspace. */

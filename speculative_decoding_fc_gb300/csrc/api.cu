@@ -920,6 +920,24 @@ dspark_status_t dspark_attention_scored(const dspark_bf16_t *q, const dspark_bf1
   return ragged_call(ragged::kScored, c, ws, ws_bytes, stream);
 }
 
+namespace {
+
+struct Region {
+  const void *at;
+  size_t bytes;
+};
+
+Region region(const void *at, long long count, size_t each) {   // (no product past 64 bits)
+  return {at, static_cast<size_t>(count) > (size_t{1} << 50) / each ? size_t{1} << 50 : count * each};
+}
+
+bool overlap(const Region &x, const Region &y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+  return x.bytes > 0 && y.bytes > 0 && (a < b ? b - a < x.bytes : a - b < y.bytes);
+}
+
+}  // namespace
+
 dspark_status_t dspark_cache_evict(const dspark_bf16_t *k_cache, const dspark_bf16_t *v_cache, const float *scores,
                                    const int32_t *lens, dspark_bf16_t *k_out, dspark_bf16_t *v_out, float *scores_out,
                                    int32_t *new_lens, int32_t *kept, int B, int nkv, int cache_len, int out_len,
@@ -935,6 +953,19 @@ dspark_status_t dspark_cache_evict(const dspark_bf16_t *k_cache, const dspark_bf
   const bool same = k_out == k_cache;
   if ((v_out == v_cache) != same || (scores_out == scores) != same || (same && out_len != cache_len) || new_lens == lens)
     return DSPARK_ERR_INVALID_ARG;
+  // what is written overlaps nothing else, but for the inputs that are cut back in place
+  const long long heads = static_cast<long long>(B) * nkv;
+  const Region in[] = {region(k_cache, heads * cache_len, 256), region(v_cache, heads * cache_len, 256),
+                       region(scores, heads * cache_len, 4), region(lens, B, 4)};
+  const Region written[] = {region(k_out, heads * out_len, 256), region(v_out, heads * out_len, 256),
+                            region(scores_out, heads * out_len, 4), region(new_lens, B, 4),
+                            region(kept, heads * budget, 4), region(status, status ? 1 : 0, 4)};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j])) return DSPARK_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j)
+      if (!(same && i == j) && overlap(written[i], in[j])) return DSPARK_ERR_INVALID_ARG;
+  }
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(scores) ||
       !aligned4(scores_out) || !aligned4(lens) || !aligned4(new_lens) || !aligned4(kept) || (status && !aligned4(status)))
     return DSPARK_ERR_MISALIGNED;
