@@ -881,6 +881,15 @@ def _int(x, name):
     return x
 
 
+def _apart(out, name, *others):
+    """An output that shares no memory with these (contiguous) tensors."""
+    a, n = out.data_ptr(), out.nbytes
+    for t in others:
+        b = t.data_ptr()
+        if a < b + t.nbytes and b < a + n:
+            raise ValueError("%s overlaps an input or another output" % name)
+
+
 def _index(t, name):
     """The device of a call: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
@@ -909,9 +918,10 @@ def qk_norm_rope_ragged(qkv, nq, nkv, q_norm_w, k_norm_w, theta, k_cache, v_cach
                         nrows=None, q_out=None, status=None, stream=None):
     """qk_norm_rope with each request at its own place: row j < nrows[b] of request b is at
     position pos[b] + j and its key and value go to cache slot slot[b] + j (slot None: pos,
-    nothing of a request at a negative one; nrows None: rows_per_req).  pos, slot, nrows: int32 [B] on the device.  Returns q
-    [rows, nq, 128] (None when nq == 0); rows past nrows[b] are left alone (a fresh q_out
-    holds zeros there).  status: optional int32 [1] that records bad places."""
+    nothing of a request at a negative one; nrows None: rows_per_req).  pos, slot, nrows:
+    int32 [B] on the device.  Returns q [rows, nq, 128] (None when nq == 0); rows past
+    nrows[b] are left alone (a fresh q_out holds zeros there).  status: optional int32 [1]
+    that records bad places."""
     if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype is not _BF16 or qkv.dim() != 2 \
             or qkv.shape[1] != (nq + 2 * nkv) * 128 or qkv.stride(1) != 1:
         raise ValueError("qkv must be a CUDA bf16 [rows, (nq + 2 nkv) * 128] tensor with unit column stride")
@@ -924,6 +934,8 @@ def qk_norm_rope_ragged(qkv, nq, nkv, q_norm_w, k_norm_w, theta, k_cache, v_cach
     wk = _dense(k_norm_w, "k_norm_w", _BF16, (128,), di)
     kc = _dense(k_cache, "k_cache", _BF16, shape, di)
     vc = _dense(v_cache, "v_cache", _BF16, shape, di)
+    if abs(kc - vc) < 256 * B * cache_len * nkv:
+        raise ValueError("k_cache and v_cache overlap")
     pp = _dense(pos, "pos", _I32, (B,), di)
     sp = None if slot is None else _dense(slot, "slot", _I32, (B,), di)
     np_ = None if nrows is None else _dense(nrows, "nrows", _I32, (B,), di)
@@ -934,6 +946,9 @@ def qk_norm_rope_ragged(qkv, nq, nkv, q_norm_w, k_norm_w, theta, k_cache, v_cach
             wq = _dense(q_norm_w, "q_norm_w", _BF16, (128,), di)
             if q_out is None:
                 q_out = (torch.empty if nrows is None else torch.zeros)((rows, nq, 128), dtype=_BF16, device=qkv.device)
+            elif q_out.data_ptr() < qkv.data_ptr() + 2 * ((rows - 1) * qkv.stride(0) + qkv.shape[1]) \
+                    and qkv.data_ptr() < q_out.data_ptr() + q_out.nbytes:
+                raise ValueError("q_out overlaps qkv")
             qp = _dense(q_out, "q_out", _BF16, (rows, nq, 128), di)
         _check(lib().dspark_qk_norm_rope_ragged(
             qkv.data_ptr(), qkv.stride(0), nq, nkv, wq, wk, float(theta), pp, sp, np_, qp, kc, vc, B, cache_len,
@@ -953,6 +968,7 @@ def _ragged_args(q, k_cache, v_cache, lens, out, di):
             _dense(v_cache, "v_cache", _BF16, shape, di), _dense(lens, "lens", _I32, (B,), di))
     if out is not None:
         _dense(out, "out", _BF16, rows, di)
+        _apart(out, "out", q, k_cache, v_cache, lens)
     return B, nr, nq, nkv, cache_len, ptrs
 
 
@@ -989,6 +1005,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, lens, causa
     P = k_prefix.shape[0]
     kpre = _dense(k_prefix, "k_prefix", _BF16, (P, nkv, 128), di)
     vpre = _dense(v_prefix, "v_prefix", _BF16, (P, nkv, 128), di)
+    if out is not None:
+        _apart(out, "out", k_prefix, v_prefix)
     with _on(di, stream):
         if out is None:
             out = torch.empty_like(q)
@@ -1014,6 +1032,8 @@ def attention_scored(q, k_cache, v_cache, lens, scores=None, decay=1.0, causal=F
         if scores_out is None:
             scores_out = scores if scores is not None else torch.zeros(shape, dtype=_F32, device=q.device)
         so = _dense(scores_out, "scores_out", _F32, shape, di)
+        if sp is not None and sp != so:
+            _apart(scores_out, "scores_out", scores)
         if out is None:
             out = torch.empty_like(q)
         ws, nbytes = _ws(workspaces, "ragged_scored", di, "dspark_attention_scored", B, nr, nq, nkv, cache_len)

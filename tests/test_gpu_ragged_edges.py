@@ -110,3 +110,30 @@ def test_negative_position_without_slots():
             want, mag = ref.rope(x[b, :, nq:nq + nkv], w, at, 1e6)
             assert ((kc[b, p:p + rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + 64 * U * mag).all()
             assert torch.equal(vc[b, p:p + rows], x[b, :, nq + nkv:])
+
+
+def test_overlapping_outputs_are_refused():
+    g = _gen(1600)
+    q, kc, vc = _normal((2, 4, 8, HD), g), _normal((2, 64, 8, HD), g), _normal((2, 64, 8, HD), g)
+    lens, sc = _lens([64, 9]), torch.zeros((2, 8, 64), device="cuda")
+    w = torch.ones(HD, dtype=torch.bfloat16, device="cuda")
+    wide = _normal((9, 24 * HD), g)   # its first 8 rows are the call's
+    two = torch.zeros((3, 8, 64), device="cuda")
+    for call in (lambda: ds.window_attention(q, kc, vc, lens, 0, out=q),
+                 lambda: ds.window_attention(q, kc, vc, lens, 0, out=vc.view(-1)[:q.numel()].view(q.shape)),
+                 lambda: ds.shared_prefix_attention(q, q[0], vc[0, :4], kc, vc, lens, out=q),
+                 lambda: ds.shared_prefix_attention(q, kc[0], wide[:4, :8 * HD].reshape(4, 8, HD), kc, vc, lens,
+                                                    out=vc.view(-1)[8 * HD:8 * HD + q.numel()].view(q.shape)),
+                 lambda: ds.attention_scored(q, kc, vc, lens, sc, out=q),
+                 lambda: ds.attention_scored(q, kc, vc, lens, two[:2], scores_out=two[1:]),
+                 lambda: ds.qk_norm_rope_ragged(wide[:8], 8, 8, w, w, 1e6, kc, kc, 4, lens),
+                 lambda: ds.qk_norm_rope_ragged(wide[:8], 8, 8, w, w, 1e6, kc, vc, 4, lens,
+                                                q_out=wide.view(-1)[HD:HD + 64 * HD].view(8, 8, HD))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    # right behind one another is apart
+    both = torch.empty((2,) + q.shape, dtype=torch.bfloat16, device="cuda")
+    both[0] = q
+    got = ds.window_attention(both[0], kc, vc, lens, 0, out=both[1])
+    assert torch.equal(got, ds.window_attention(q, kc, vc, lens, 0)) and torch.equal(both[0], q)
+    assert ds.attention_scored(q, kc, vc, lens, sc, scores_out=sc)[1] is sc

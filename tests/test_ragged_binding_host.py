@@ -29,3 +29,11 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         ds._on(0, Stream())
+
+
+def test_outputs_share_no_memory():
+    x = torch.zeros(100)
+    ds._apart(x[:50], "out", x[50:])
+    for a, b in ((x, x), (x[:51], x[50:]), (x[50:], x[:51]), (x[10:20], x)):
+        with pytest.raises(ValueError, match="out overlaps"):
+            ds._apart(a, "out", b)
