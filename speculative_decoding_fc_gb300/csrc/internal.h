@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dspark.h"
 
 namespace dspark {
@@ -183,6 +185,19 @@ template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args &&...args) {
   return launch_kernel(true, kernel, grid, block, smem, stream, static_cast<Args &&>(args)...);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (calls may come from
+// several threads: setting it twice does no harm).
+template <typename Kernel>
+bool allow_smem(Kernel kernel, size_t bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return false;
+  done[dev].store(true, std::memory_order_release);
+  return true;
 }
 
 // ------------------------------------------------------------------ launch accounting

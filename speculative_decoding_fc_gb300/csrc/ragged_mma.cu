@@ -664,14 +664,8 @@ dspark_status_t mma_launch(const Args &a, bool scored, cudaStream_t stream) {
   if (a.PRT > 0 && (!cache_map(&prm.kp, a.k_prefix, 1, a.P, a.nkv, kKT) || !cache_map(&prm.vp, a.v_prefix, 1, a.P, a.nkv, kKT)))
     return DSPARK_ERR_UNSUPPORTED_SHAPE;
   auto kern = scored ? ragged_mma_kernel<true> : ragged_mma_kernel<false>;
-  static bool done[2][64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSPARK_ERR_CUDA;
-  if (!done[scored][dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return DSPARK_ERR_CUDA;
-    done[scored][dev] = true;
-  }
+  static std::atomic<bool> done[2][64];
+  if (!allow_smem(kern, kSmem, done[scored])) return DSPARK_ERR_CUDA;
   if (launch_pdl(kern, dim3(static_cast<unsigned>(a.groups * a.nkv)), dim3(kThreads), kSmem, stream, prm) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   count_launches(1);

@@ -754,14 +754,8 @@ dspark_status_t tc_launch(const Args &a, Form form, cudaStream_t stream) {
     if (a.PRT > 0 && !rows_map(&prm.qp, a.q, a.B * a.nr, a.nq, a.grp, a.B * a.nr)) return DSPARK_ERR_CUDA;
   }
   auto kern = streams ? ragged_tc_kernel<true> : ragged_tc_kernel<false>;
-  static bool done[2][64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSPARK_ERR_CUDA;
-  if (!done[streams][dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return DSPARK_ERR_CUDA;
-    done[streams][dev] = true;
-  }
+  static std::atomic<bool> done[2][64];
+  if (!allow_smem(kern, kSmem, done[streams])) return DSPARK_ERR_CUDA;
   const int ctas = (streams ? (a.groups + 1) / 2 : a.groups) * a.nkv;
   if (launch_kernel(!a.ordinary, kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, stream, prm) !=
       cudaSuccess)

@@ -258,14 +258,8 @@ dspark_status_t weights_launch(const Args &a, cudaStream_t stream) {
   WeightParams prm;
   prm.a = a;
   if (!cache_map(&prm.k, a.k_cache, a.B, a.cache_len, a.nkv, kKT)) return DSPARK_ERR_UNSUPPORTED_SHAPE;
-  static bool done[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSPARK_ERR_CUDA;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(ragged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return DSPARK_ERR_CUDA;
-    done[dev] = true;
-  }
+  static std::atomic<bool> done[64];
+  if (!allow_smem(ragged_weights_kernel, kSmem, done)) return DSPARK_ERR_CUDA;
   if (launch_pdl(ragged_weights_kernel, dim3(static_cast<unsigned>(a.groups * a.nkv)), dim3(kThreads), kSmem,
                  stream, prm) != cudaSuccess)
     return DSPARK_ERR_CUDA;

@@ -6,6 +6,8 @@ is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together
 parts' products are added in fp32, 2 n additions over n keys:
   |err| <= 2^-8 |out| (1 + w) + w sum p|v|,  w = 260 u A + 2^-16 + 2^-19 + 2 n u.
 """
+import threading
+
 import pytest
 import torch
 
@@ -137,3 +139,48 @@ def test_overlapping_outputs_are_refused():
     got = ds.window_attention(both[0], kc, vc, lens, 0, out=both[1])
     assert torch.equal(got, ds.window_attention(q, kc, vc, lens, 0)) and torch.equal(both[0], q)
     assert ds.attention_scored(q, kc, vc, lens, sc, scores_out=sc)[1] is sc
+
+
+def test_calls_from_two_threads():
+    """Host threads with streams and workspaces of their own, each form and the append."""
+    g = _gen(1700)
+    w = torch.ones(HD, dtype=torch.bfloat16, device="cuda")
+    sets = []
+    for i in range(2):
+        kc, vc = _normal((4, 300, 4, HD), g), _normal((4, 300, 4, HD), g)
+        sets.append((kc, vc, _lens([300, 1, 64 + i, 200]), [_normal((4, n, 8, HD), g) for n in (1, 9, 40)],
+                     _normal((32, 16 * HD), g), torch.zeros((2, 4, 320, 4, HD), dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+
+    def work(i, stream, spaces, got):
+        kc, vc, lens, qs, qkv, new = sets[i]
+        for _ in range(3):
+            for q in qs:
+                got.append(ds.window_attention(q, kc, vc, lens, 0, stream=stream, workspaces=spaces))
+                got.append(ds.shared_prefix_attention(q, kc[0], vc[0], kc, vc, lens, stream=stream, workspaces=spaces))
+                if q.shape[1] < 32:
+                    got.extend(ds.attention_scored(q, kc, vc, lens, stream=stream, workspaces=spaces))
+            got.append(ds.qk_norm_rope_ragged(qkv, 8, 4, w, w, 1e6, new[0], new[1], 8, lens, stream=stream))
+
+    want, got, failed = [[], []], [[], []], []
+    for i in range(2):
+        work(i, torch.cuda.Stream(), ds.Workspaces(), want[i])
+        torch.cuda.synchronize()
+
+    def run(i):
+        try:
+            work(i, torch.cuda.Stream(), ds.Workspaces(), got[i])
+        except Exception as e:   # (a thread's exception would be lost)
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in range(2):
+        assert len(got[i]) == len(want[i])
+        for x, y in zip(got[i], want[i]):
+            assert torch.equal(x, y)
