@@ -1,5 +1,5 @@
 """Ragged-batch operators where their kernels and schedules change: weights in two parts,
-places without a slot, data written right before a call.
+prefixes over many ranges, places without a slot, data written right before a call.
 
 Tolerances as derived in test_gpu_ragged.py, for weights of two bf16 parts: the low part
 is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together.  Both
@@ -48,6 +48,74 @@ def test_weights_of_blocks_have_two_parts(case):
     _close2(ds.window_attention(q, kc, vc, _lens(lens), window, sinks=sinks, causal=causal), want, av, a, cache)
     if not window:
         _close2(ds.attention_scored(q, kc, vc, _lens(lens), causal=causal)[0], want, av, a, cache)
+
+
+PREFIX_CASES = [
+    # B, nr, nq, nkv, P, cache, lens, causal
+    (3, 1, 40, 8, 4096, 70, [0, 64, 70], True),            # 15 rows: the decode kernel, many ranges
+    (1, 2, 40, 8, 1025, 70, [2], False),
+    (2, 1, 40, 8, 20000, 130, [130, 0], True),             # ... with the cost of changing items
+    (1, 1, 16, 1, 3333, 65, [65], True),
+    (4, 1, 40, 8, 4096, 70, [0, 1, 64, 70], True),         # 20 rows: tcgen05, four warps to a row in the join
+    (1, 8, 40, 8, 20000, 130, [130], True),
+    (1, 8, 40, 8, 20000, 130, [0], False),
+    (12, 1, 40, 8, 1031, 300, [25 * b for b in range(12)], True),   # 60 rows
+    (64, 1, 8, 8, 2500, 70, [(9 * b) % 71 for b in range(64)], True),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PREFIX_CASES)))
+def test_few_rows_over_a_long_prefix(case):
+    B, nr, nq, nkv, P, cache, lens, causal = PREFIX_CASES[case]
+    g = _gen(1100 + case)
+    q = _normal((B, nr, nq, HD), g, 1.5)
+    kp, vp = _normal((P, nkv, HD), g), _normal((P, nkv, HD), g)
+    kc, vc = _normal((B, cache, nkv, HD), g), _normal((B, cache, nkv, HD), g)
+    _hide(kc, vc, nr, lens, 0, 0, causal)
+    want, av, a = ref.prefix(q, kp, vp, kc, vc, lens, causal)
+    out = ds.shared_prefix_attention(q, kp, vp, kc, vc, _lens(lens), causal=causal)
+    _close2(out, want, av, a, P + cache)
+    assert torch.equal(out, ds.shared_prefix_attention(q, kp, vp, kc, vc, _lens(lens), causal=causal))
+
+
+@pytest.mark.parametrize("P", [500, 4096, 20000])
+def test_prefix_schedule_found_by_warps_and_by_the_plan(P):
+    """32 requests (each warp works its range out) and the same with an empty one behind them
+    (the plan kernel does): the same kernel and ranges, so the same bits."""
+    g = _gen(1200 + P)
+    B, n, nkv, cache = 33, 32, 8, 90
+    lens = [(13 * b * b + 7) % 91 for b in range(n)] + [0]
+    q = _normal((B, 1, nkv, HD), g, 1.5)
+    kp, vp = _normal((P, nkv, HD), g), _normal((P, nkv, HD), g)
+    kc, vc = _normal((B, cache, nkv, HD), g), _normal((B, cache, nkv, HD), g)
+    want, av, a = ref.prefix(q, kp, vp, kc, vc, lens, True)
+    full = ds.shared_prefix_attention(q, kp, vp, kc, vc, _lens(lens), causal=True)
+    _close2(full, want, av, a, P + cache)
+    assert torch.equal(full[:n], ds.shared_prefix_attention(q[:n], kp, vp, kc[:n], vc[:n], _lens(lens[:n]), causal=True))
+
+
+@pytest.mark.parametrize("B,nr", [(3, 1), (6, 1), (40, 8), (6, 8)])
+def test_lengths_out_of_range_with_a_prefix_and_with_scores(B, nr):
+    g = _gen(1300 + B + nr)
+    nq, nkv, cache, P = 40, 8, 80, 600
+    q = _normal((B, nr, nq, HD), g)
+    kp, vp = _normal((P, nkv, HD), g), _normal((P, nkv, HD), g)
+    kc, vc = _normal((B, cache, nkv, HD), g), _normal((B, cache, nkv, HD), g)
+    for bad in (-1, cache + 1):
+        lens = [(11 * b + 3) % (cache + 1) for b in range(B)]
+        lens[B - 2] = bad
+        good = [min(max(n, 0), cache) for n in lens]
+        spaces = ds.Workspaces()
+        out = ds.shared_prefix_attention(q, kp, vp, kc, vc, _lens(lens), workspaces=spaces)
+        assert ds.workspace_status(spaces.buffer("ragged_prefix", q.device)) == -1
+        assert torch.equal(out, ds.shared_prefix_attention(q, kp, vp, kc, vc, _lens(good), workspaces=spaces))
+        assert ds.workspace_status(spaces.buffer("ragged_prefix", q.device)) == 0
+        sc = torch.rand((B, nkv, cache), device="cuda", generator=g)
+        out, new = ds.attention_scored(q, kc, vc, _lens(lens), sc.clone(), workspaces=spaces)
+        assert ds.workspace_status(spaces.buffer("ragged_scored", q.device)) == -1
+        out1, new1 = ds.attention_scored(q, kc, vc, _lens(good), sc.clone(), workspaces=spaces)
+        assert torch.equal(out, out1) and torch.equal(new, new1)
+        assert ds.workspace_status(spaces.buffer("ragged_scored", q.device)) == 0
 
 
 @pytest.mark.parametrize("graph", [False, True])
