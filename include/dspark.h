@@ -609,8 +609,15 @@ dspark_status_t dspark_backbone_block(const int32_t *tokens, int B, int nr, cons
  * bf16 once (each off by up to 2^-8 relative).  Results do not depend on timing.
  * Outputs must not overlap inputs except where a call says so.
  * Limits: nq % nkv == 0, nq <= 4096, nkv <= 1024, B <= 2^16, B * nr <= 2^20,
- * cache_len <= 2^30.
- * Workspaces need no zeroing but for the status word (their first 4 bytes).
+ * cache_len <= 2^30, window and sinks <= 2^30; and the row tiles (of 16, 64 or 256 rows: up
+ * to 16, up to 64, more than 64 rows of a kv head) times the 64-key tiles of cache_len, over
+ * all requests and the prefix, below 2 * 10^9.
+ * Workspaces need no zeroing but for the status word (their first 4 bytes).  They hold the
+ * schedule and the pieces of split rows (5, 20 or 41 MB by those row counts, up to twice that
+ * for hundreds of kv heads; the scored form 41 MB more); with a prefix also 1 KB per query
+ * row and head; the scored form for up to 16 rows of a kv head 4 bytes per query row, head
+ * and slot of the caches, whatever the lengths (64 requests of 40 heads over 131072 slots:
+ * 1.4 GB, with 3 rows each 4.1 GB).
  * ======================================================================== */
 
 /* dspark_qk_norm_rope with each request at its own place: row j < nrows[b] of request b
@@ -673,6 +680,8 @@ dspark_status_t dspark_attention_scored(const dspark_bf16_t *q, const dspark_bf1
  *     input otherwise, or another output;
  *   new_lens [B] int32 (not lens itself); kept [B, nkv, budget] int32: the old slots, then
  *     -1.  sinks + recent <= budget, cache_len <= 2^22.  status: a device int32 or NULL.
+ * In place, the scores of slots from m on stay the old keys': set them to zero before
+ * dspark_attention_scored goes on counting for the keys that come there.
  * Two kernels, no workspace. */
 dspark_status_t dspark_cache_evict(const dspark_bf16_t *k_cache, const dspark_bf16_t *v_cache, const float *scores,
                                    const int32_t *lens, dspark_bf16_t *k_out, dspark_bf16_t *v_out, float *scores_out,

@@ -1049,8 +1049,9 @@ def cache_evict(k_cache, v_cache, scores, lens, budget, sinks=0, recent=0, k_out
     `recent` and, between them, those with the largest scores (equal scores: the lower slot)
     move in ascending order to slots 0 .. m - 1, m = min(lens[b], budget), with their values
     and scores.  Into k_out, v_out [B, out_len, nkv, 128] and scores_out [B, nkv, out_len] (all
-    three given), else in place; slots from m on are left alone.  Returns (new_lens [B] int32,
-    kept [B, nkv, budget] int32: the old slots, then -1)."""
+    three given), else in place; slots from m on are left alone (their scores too: zero them
+    before attention_scored goes on counting for new keys there).  Returns (new_lens [B]
+    int32, kept [B, nkv, budget] int32: the old slots, then -1)."""
     budget, sinks, recent = _int(budget, "budget"), _int(sinks, "sinks"), _int(recent, "recent")
     di = _index(k_cache, "k_cache")
     if k_cache.dim() != 4:

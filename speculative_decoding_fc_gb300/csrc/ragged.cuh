@@ -22,9 +22,9 @@
 // the DRAM pages it opens to be opened again for every other head.  ragged_plan_kernel
 // works the ranges out from the lengths on the device (a captured graph follows them); the
 // other kernels read where their range begins.  (Each CTA finding its own place took 3 to 8
-// us of dependent loads and shuffles, the plan kernel about 3 us once.)  Up to 32 items each
+// us of dependent loads and shuffles, the plan kernel about 3 us once, 6 with cold caches.)  Up to 32 items each
 // warp that needs its range has one lane per item work it out instead (WarpPlan) and the plan's
-// launch is left out: one draft block over 1032 keys 13.6 -> 11.2 us, 32 single tokens 74.2 ->
+// launch is left out: one draft block over 1032 keys took 2.4 us less, 32 single tokens 74.2 ->
 // 71.8.
 // An item held by one range is finished there; every other item leaves pieces
 // (unnormalised fp32 output, row maximum and sum), at most two per range and head (the

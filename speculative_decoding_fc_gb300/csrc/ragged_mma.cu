@@ -490,9 +490,10 @@ __device__ __forceinline__ void join_parts(RowSum &s, int lane, int part) {
 
 // A row's result is the sum over its pieces e^(m - M) o / sum e^(m - M) l, taken in order,
 // one warp per row; items that one range held are finished already; the rows of row tiles
-// without keys become zero.  kBatch: pieces of a row loaded together.  Bound by latency (4 us
-// for single tokens and blocks; with a prefix 14 us at 32 x 8 queries of 40 heads, 32 us at
-// 192 x 8, which read 64 MB and more of fp32 rows and pieces).
+// without keys become zero.  kBatch: pieces of a row loaded together.  Bound by latency
+// (with cold caches 4.4 us for 64 single tokens, 5 to 9 for one block; with a prefix 14 us
+// at 32 x 8 queries of 40 heads, 32 to 35 at 192 x 8, which read 64 MB and more of fp32 rows and
+// pieces).
 //
 // Few items (no more than ranges: spread over many of them, each batch of pieces a round trip
 // to L2): CTA (item and kv head, 8 / kSplit rows), kSplit warps to a row.
@@ -585,7 +586,8 @@ __global__ void __launch_bounds__(256, kBatch == 4 ? 4 : 1) ragged_join_prefix_k
 // ------------------------------------------------------------------ column sums
 // scores_out[b, g, t] = decay * scores_in[b, g, t] + sum over the group's rows of the
 // weight e^(s - M) / L, t < len, from the row scores that the decode kernel left (at most
-// 64 bytes a key, in L2 still); rows in order.  CTA (2048 keys of a kv head: with 512, most
+// 64 bytes a key and kv head: in L2 still at the sizes below, 15 MB; more than 129 MB of them
+// come from memory); rows in order.  CTA (2048 keys of a kv head: with 512, most
 // of the time went by in CTAs behind the requests' ends), a thread's four key pairs together
 // (one after the other they waited for each other's loads: 32 requests of 8 kv heads and 93
 // thousand keys, 5 rows, 16.6 us; together 10.8).
@@ -674,8 +676,8 @@ dspark_status_t mma_launch(const Args &a, bool scored, cudaStream_t stream) {
 
 dspark_status_t join_launch(const Args &a, int rw, bool scored, cudaStream_t stream) {
   // four warps to a row where it may have more pieces than one loads together (4 tokens over a
-  // prefix of 4096 19.2 -> 16.2 us, a scored block over 2057 keys 23.2 -> 21.2; with 9 pieces, a
-  // block with a window of 512, 11.3 -> 12.5: not there)
+  // prefix of 4096 3 us less, a scored block over 2057 keys 2 us less; with 9 pieces, a block
+  // with a window of 512, 1.2 us more: not there)
   constexpr int kSplit = 4, kBatch = 16;
   cudaError_t e;
   if (a.P > 0) {

@@ -23,11 +23,13 @@
 // work while the softmax computes.  (With tiles of 128 keys S filled its half's columns, P had
 // to take its place, and products and softmax of a half took turns: 3500 cycles per 128 keys
 // of both halves, of which the pipe worked 2050.)
-// Measured: 1536 rows of 40 heads over a prefix of 32749 keys, 1.03 TFLOP in 733 us: 1.40
+// Measured: 1536 rows of 40 heads over a prefix of 32749 keys, 1.03 TFLOP in 731 us: 1.41
 // PFLOP/s, 72% of the bf16 peak measured with a large library product; 1710 cycles per 64
-// keys of both halves, in which the pipe has 1024 of work and a softmax about 1100.  What
-// bounds it is neither alone but the way between them (barriers, tensor memory, the MMA
-// warps' own loop).  Tried and slower: a lock that keeps one half's MMAs together, half 0's Q
+// keys of both halves (counts of cycles: clock64 in builds made for it).  Products take 1024
+// of them, at 128 bytes a cycle the shared-memory reads of Q and K (48 KB for each half's 256
+// cycles of Q K^T) hold the pipe about 256 longer, and a softmax takes about 1100; over a
+// prefix of 16384 the pipe is active 56% of the time.  What bounds it is neither alone but the
+// way between them (barriers, tensor memory, the MMA warps' own loop).  Tried and slower: a lock that keeps one half's MMAs together, half 0's Q
 // in tensor memory with one buffer of P, four warpgroups of softmax with two threads a row,
 // the ring's stages given back by the softmax warps instead of a commit each.
 // The output is rescaled only when a row's maximum has grown by more than 2^8 since the
