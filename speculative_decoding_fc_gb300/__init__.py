@@ -946,10 +946,13 @@ def qk_norm_rope_ragged(qkv, nq, nkv, q_norm_w, k_norm_w, theta, k_cache, v_cach
             wq = _dense(q_norm_w, "q_norm_w", _BF16, (128,), di)
             if q_out is None:
                 q_out = (torch.empty if nrows is None else torch.zeros)((rows, nq, 128), dtype=_BF16, device=qkv.device)
-            elif q_out.data_ptr() < qkv.data_ptr() + 2 * ((rows - 1) * qkv.stride(0) + qkv.shape[1]) \
-                    and qkv.data_ptr() < q_out.data_ptr() + q_out.nbytes:
-                raise ValueError("q_out overlaps qkv")
-            qp = _dense(q_out, "q_out", _BF16, (rows, nq, 128), di)
+                qp = q_out.data_ptr()
+            else:
+                qp = _dense(q_out, "q_out", _BF16, (rows, nq, 128), di)
+                if qp < qkv.data_ptr() + 2 * ((rows - 1) * qkv.stride(0) + qkv.shape[1]) \
+                        and qkv.data_ptr() < qp + q_out.nbytes:
+                    raise ValueError("q_out overlaps qkv")
+                _apart(q_out, "q_out", k_cache, v_cache)
         _check(lib().dspark_qk_norm_rope_ragged(
             qkv.data_ptr(), qkv.stride(0), nq, nkv, wq, wk, float(theta), pp, sp, np_, qp, kc, vc, B, cache_len,
             rows_per_req, st, _raw_stream(di)), "dspark_qk_norm_rope_ragged")
