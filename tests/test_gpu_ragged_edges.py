@@ -5,6 +5,10 @@ Tolerances as derived in test_gpu_ragged.py, for weights of two bf16 parts: the 
 is off by 2^-8 of what the high part left, 2^-8 of the weight, so 2^-16 together.  Both
 parts' products are added in fp32, 2 n additions over n keys:
   |err| <= 2^-8 |out| (1 + w) + w sum p|v|,  w = 260 u A + 2^-16 + 2^-19 + 2 n u.
+Append: beside the roundings of the two products, the angle, below 2 pi, is rounded to fp32
+(at most 2^-22 = 4 u off), and a sine or cosine moves by as much whatever its own size, as it
+does by the function's error (below 4 u): 8 u of each unrotated value, near a zero of the
+cosine far more than 64 u of the product.
 """
 import threading
 
@@ -158,6 +162,15 @@ def test_shared_prefix_of_data_written_right_before(B, nr, nq, nkv, P, cache, gr
         assert torch.equal(x, want[i % 4])
 
 
+def _rotated_close(got, x, w, at):
+    want, mag = ref.rope(x, w, at, 1e6)
+    y = x.double()
+    y = (y / torch.sqrt(y.square().mean(-1, keepdim=True) + 1e-6) * w.double()).abs()
+    pair = y[..., :64] + y[..., 64:]
+    bound = 2.0 ** -8 * want.abs() + 64 * U * mag + 8 * U * torch.cat([pair, pair], -1)
+    assert ((got.double() - want).abs() <= bound).all()
+
+
 def test_negative_position_without_slots():
     """No slot given: a request at a negative position has none, and nothing of it is stored."""
     g = _gen(1500)
@@ -174,11 +187,9 @@ def test_negative_position_without_slots():
     x = qkv.view(B, rows, nq + 2 * nkv, HD)
     for b, p in enumerate([5, 0, 2]):   # queries: a negative position counts as 0
         at = torch.arange(rows, device="cuda") + p
-        want, mag = ref.rope(x[b, :, :nq], w, at, 1e6)
-        assert ((q.view(B, rows, nq, HD)[b].double() - want).abs() <= 2.0 ** -8 * want.abs() + 64 * U * mag).all()
+        _rotated_close(q.view(B, rows, nq, HD)[b], x[b, :, :nq], w, at)
         if b != 1:
-            want, mag = ref.rope(x[b, :, nq:nq + nkv], w, at, 1e6)
-            assert ((kc[b, p:p + rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + 64 * U * mag).all()
+            _rotated_close(kc[b, p:p + rows], x[b, :, nq:nq + nkv], w, at)
             assert torch.equal(vc[b, p:p + rows], x[b, :, nq + nkv:])
 
 
@@ -252,3 +263,19 @@ def test_calls_from_two_threads():
         assert len(got[i]) == len(want[i])
         for x, y in zip(got[i], want[i]):
             assert torch.equal(x, y)
+
+
+def test_append_over_far_positions():
+    """Many rows at positions up to a million: some pairs stand where the cosine is near zero."""
+    g = _gen(1800)
+    B, rows, nq, nkv = 200, 9, 20, 4
+    kc, vc = (torch.zeros((B, rows, nkv, HD), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qkv = _normal((B * rows, (nq + 2 * nkv) * HD), g, 2.0)
+    w = (1.0 + _normal((HD,), g, 0.1, torch.float32)).bfloat16()
+    pos = [(4999 * b * b + 17 * b) % 1000003 for b in range(B)]
+    q = ds.qk_norm_rope_ragged(qkv, nq, nkv, w, w, 1e6, kc, vc, rows, _lens(pos), slot=_lens([0] * B))
+    at = (_lens(pos)[:, None] + torch.arange(rows, device="cuda")).view(-1)
+    x = qkv.view(B * rows, nq + 2 * nkv, HD)
+    _rotated_close(q, x[:, :nq], w, at)
+    _rotated_close(kc.view(B * rows, nkv, HD), x[:, nq:nq + nkv], w, at)
+    assert torch.equal(vc.view(B * rows, nkv, HD), x[:, nq + nkv:])
